@@ -5,13 +5,17 @@ take raw integers (device pointers, sizes, a cudaStream_t handle) and return
 the C status.  ``quantize`` / ``gemm`` wrap them for torch CUDA tensors:
 they allocate outputs with torch, check every buffer they are given against
 the shape, dtype and device the call reads or writes, pass pointers and the
-current stream, and raise ``NVFP4Error`` on a non-OK status.  Every step of the computation runs
+current stream (or the one that they are given: what they allocate then belongs
+to that one, and the caller waits for it before using the results), and raise
+``NVFP4Error`` on a non-OK status.  Every step of the computation runs
 in the library's kernels; there is no CPU or PyTorch fallback, and importing
 this module on a machine without the built library raises at first use.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 from dataclasses import dataclass
@@ -292,6 +296,55 @@ def _check(status: int, what: str) -> None:
         raise NVFP4Error(status, what)
 
 
+def _tensors(value):
+    """The torch tensors in an argument or a result of the calls below."""
+    import torch
+
+    if isinstance(value, torch.Tensor):
+        yield value
+    elif isinstance(value, (NVFP4Tensor, GatedCheckpoint)):
+        yield from _tensors(tuple(vars(value).values()))
+    elif isinstance(value, (tuple, list)):
+        for v in value:
+            yield from _tensors(v)
+
+
+def _on_stream(fn):
+    """A call whose ``stream`` may be another than the current one.  It then runs
+    with that stream current, so that what it allocates comes from that stream's
+    memory (a block of the current stream's may still be in use by work queued
+    there) and what it enqueues beside its kernels follows the same order.  Its
+    tensors are kept from reuse until the given stream is done with them, its
+    results until the current stream is: the caller waits for the stream before
+    using them, and may drop them like any others."""
+    params = inspect.signature(fn).parameters
+    at = list(params).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        import torch
+
+        current = torch.cuda.current_stream(stream.device)
+        if stream == current:
+            return fn(*args, **kwargs)
+        given = list(_tensors((args, tuple(kwargs.values()))))
+        for t in given:
+            if t.is_cuda and t.device != stream.device:
+                raise ValueError(f"stream is on {stream.device}, the buffers are on {t.device}")
+        with torch.cuda.stream(stream):
+            result = fn(*args, **kwargs)
+        for t in given:
+            t.record_stream(stream)
+        for t in _tensors(result):
+            t.record_stream(current)
+        return result
+
+    return call
+
+
 # The C ABI takes raw pointers and cannot see buffer sizes, so the wrappers
 # check every torch buffer they pass against the shape the call will read or
 # write: a buffer that is too small, of another dtype or on another device is
@@ -363,6 +416,7 @@ def _out_code(out_dtype, out):
     return out_dtype, codes[out_dtype]
 
 
+@_on_stream
 def quantize(x, mode: str = "six", rule: str = "max", fp8_max: float | None = None,
              out: NVFP4Tensor | None = None, stream=None, global_scale=None) -> NVFP4Tensor:
     """NVFP4-quantize a CUDA bf16 matrix [rows, K] (K % 64 == 0).
@@ -414,6 +468,7 @@ AUG_RESIDUAL = 0
 AUG_DUPLICATE = 1
 
 
+@_on_stream
 def quantize_arc(x, perm, S: int, augment: int = AUG_RESIDUAL, mode: str = "six", rule: str = "max",
                  fp8_max: float | None = None, out: NVFP4Tensor | None = None, stream=None) -> NVFP4Tensor:
     """ARCQuant augmented quantization of a CUDA bf16 matrix x [rows, K]:
@@ -451,6 +506,7 @@ def quantize_arc(x, perm, S: int, augment: int = AUG_RESIDUAL, mode: str = "six"
     return out
 
 
+@_on_stream
 def quantize_arc_rmsnorm(x, gamma, eps: float, perm, S: int, mode: str = "six", rule: str = "max",
                          fp8_max: float | None = None, out: NVFP4Tensor | None = None, stream=None) -> NVFP4Tensor:
     """``quantize_arc`` (residual channels) of the RMSNorm of x: the rows of
@@ -490,6 +546,7 @@ def quantize_arc_rmsnorm(x, gamma, eps: float, perm, S: int, mode: str = "six", 
     return out
 
 
+@_on_stream
 def quantize_t(x, mode: str = "six", rule: str = "max", fp8_max: float | None = None,
                out: NVFP4Tensor | None = None, stream=None) -> NVFP4Tensor:
     """NVFP4-quantize x^T for a CUDA bf16 matrix x [rows, K] (rows % 64 == 0,
@@ -518,6 +575,7 @@ def quantize_t(x, mode: str = "six", rule: str = "max", fp8_max: float | None = 
     return out
 
 
+@_on_stream
 def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out_dtype=None, out=None, workspace=None,
          stream=None):
     """Y[M, N] = A_hat @ B_hat^T for two NVFP4 operands with the same K."""
@@ -544,6 +602,7 @@ def gemm(a: NVFP4Tensor, b: NVFP4Tensor, out_dtype=None, out=None, workspace=Non
     return out
 
 
+@_on_stream
 def quantize_gemm(x, w: NVFP4Tensor, mode: str = "six", rule: str = "max", fp8_max: float | None = None,
                   out_dtype=None, x_out: NVFP4Tensor | None = None, out=None, workspace=None, stream=None):
     """The W4A4 linear layer in one call: quantize the bf16 CUDA activations
@@ -588,6 +647,7 @@ def quantize_gemm(x, w: NVFP4Tensor, mode: str = "six", rule: str = "max", fp8_m
     return x_out, out
 
 
+@_on_stream
 def quantize_arc_gemm(x, perm, S: int, w: NVFP4Tensor, mode: str = "six", rule: str = "max",
                       fp8_max: float | None = None, out_dtype=None, x_out: NVFP4Tensor | None = None, out=None,
                       workspace=None, stream=None, gamma=None, eps: float = 1e-6):
@@ -654,6 +714,7 @@ def quantize_arc_gemm(x, perm, S: int, w: NVFP4Tensor, mode: str = "six", rule: 
     return x_out, out
 
 
+@_on_stream
 def gemm_quantized(a: NVFP4Tensor, b: NVFP4Tensor, y_alpha, mode: str = "six", rule: str = "max",
                    out: NVFP4Tensor | None = None, stream=None) -> NVFP4Tensor:
     """Y = A_hat @ B_hat^T written directly as an NVFP4 [M, N] operand,
@@ -684,6 +745,7 @@ def gemm_quantized(a: NVFP4Tensor, b: NVFP4Tensor, y_alpha, mode: str = "six", r
     return out
 
 
+@_on_stream
 def gemm_segmented(a: NVFP4Tensor, b: NVFP4Tensor, b_globals, seg_ends, out_dtype=None, out=None,
                    workspace=None, stream=None):
     """Y = A_hat @ B_hat^T where B is several weights fused along N: columns
@@ -833,6 +895,7 @@ def gemv(x, w: NVFP4Tensor, out_dtype=None, out=None, stream=None):
     return _gemv(x, w, out_dtype, out, stream)
 
 
+@_on_stream
 def _gemv(x, w, out_dtype, out, stream):
     M, K, ldx = _check_rows(x, "x", (_T or _torch()).bfloat16)
     N, index = w.rows, x.get_device()
@@ -858,6 +921,7 @@ def gemv_gated(x, w_gate: NVFP4Tensor, w_up: NVFP4Tensor, act: str = "silu", out
     return _gemv_gated(x, w_gate, w_up, act, out_dtype, out, stream)
 
 
+@_on_stream
 def _gemv_gated(x, w_gate, w_up, act, out_dtype, out, stream):
     M, K, ldx = _check_rows(x, "x", (_T or _torch()).bfloat16)
     N, index = w_gate.rows, x.get_device()
@@ -923,6 +987,7 @@ def gemm_gated(a: NVFP4Tensor, w_gate: NVFP4Tensor, w_up: NVFP4Tensor, act: str 
     return _gemm_gated(a, w_gate, w_up, act, out_dtype, out, checkpoint, workspace, stream)
 
 
+@_on_stream
 def _gemm_gated(a, w_gate, w_up, act, out_dtype, out, checkpoint, workspace, stream):
     torch = _T or _torch()
     if w_gate.K != a.K or w_up.K != a.K:
@@ -975,6 +1040,7 @@ def gated_backward(dh, checkpoint: GatedCheckpoint, recompute: bool = False, out
     return _gated_backward(dh, checkpoint, recompute, out, h_out, stream)
 
 
+@_on_stream
 def _gated_backward(dh, checkpoint, recompute, out, h_out, stream):
     torch = _T or _torch()
     M, N, ldd = _check_rows(dh, "dh", torch.bfloat16)
