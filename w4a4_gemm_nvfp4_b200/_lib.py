@@ -808,7 +808,10 @@ def _fast():
     if _F is None:
         load()
         try:
-            from . import _fastcall as _F
+            from . import _fastcall as fast
+
+            # its accesses to tensors are compiled for one torch's classes
+            _F = fast if getattr(fast, "built_for", None) == str(_torch().__version__) else False
         except ImportError:
             _F = False
     return _F

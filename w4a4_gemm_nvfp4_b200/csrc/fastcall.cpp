@@ -261,5 +261,11 @@ extern "C" __attribute__((visibility("default"))) PyObject* PyInit__fastcall() {
   s_rows = PyUnicode_InternFromString("rows");
   s_K = PyUnicode_InternFromString("K");
   if (!d_bf16 || !d_f32 || !s_codes || !s_scales || !s_global_scale || !s_rows || !s_K) return nullptr;
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  // the torch that this was compiled for: the package uses it with no other
+  if (m && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
 }
