@@ -80,6 +80,8 @@ _SIGNATURES = {
     "nvfp4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "nvfp4_last_error_message": (ctypes.c_char_p, []),
     "nvfp4_testing_set_gemm_wait": (None, [ctypes.c_uint64, ctypes.c_int]),
+    "nvfp4_testing_gemv_plan": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int,
+                                               ctypes.POINTER(ctypes.c_int)]),
 }
 
 _lock = threading.Lock()
@@ -265,6 +267,13 @@ def status_string(status: int) -> str:
 
 def last_error_message() -> str:
     return load().nvfp4_last_error_message().decode()
+
+
+def testing_gemv_plan(M: int, N: int, K: int, weights: int = 1, sms: int = 148) -> dict:
+    plan = (ctypes.c_int * 5)()
+    if not load().nvfp4_testing_gemv_plan(M, N, K, weights, sms, plan):
+        raise ValueError("sizes out of range")
+    return dict(zip(("grid", "ranks", "piece_steps", "pieces", "depth"), plan))
 
 
 def testing_set_gemm_wait(timeout_ns: int = 0, debug_flags: int = 0) -> None:

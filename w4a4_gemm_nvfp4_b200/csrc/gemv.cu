@@ -50,6 +50,7 @@
 #include "block_step.cuh"  // packed pairs (f2)
 #include "common.cuh"
 #include "gated.cuh"
+#include "nvfp4_testing.h"
 
 namespace nvfp4 {
 namespace {
@@ -639,6 +640,9 @@ GemvPlan plan_gemv(uint32_t tiles, uint32_t steps, uint32_t M, uint32_t mats, ui
   return g;
 }
 
+// Row tiles of N weight rows: 8 for each 128 rows, in the last 128 those that hold a row.
+uint32_t row_tiles(int64_t N) { return static_cast<uint32_t>(N / 128 * 8 + std::min<int64_t>(8, (N % 128 + 3) / 4)); }
+
 template <int NT, bool GATED, int D, int R>
 cudaError_t launch_gemv(int dev, const GemvPlan& plan, cudaStream_t s, const GemvParams& p) {
   static PerContextCache<int> attr;
@@ -723,8 +727,7 @@ nvfp4_status gemv_impl(const char* fn, const void* x, int64_t M, int64_t K, int6
   p.act = act;
   p.out_fp32 = out_dtype == NVFP4_OUT_FP32;
   p.x_vec = aligned16(x) && ldx % 8 == 0;
-  // row tiles: 8 for each 128 rows, in the last 128 those that hold a row
-  const uint32_t tiles = static_cast<uint32_t>(N / 128 * 8 + std::min<int64_t>(8, (N % 128 + 3) / 4));
+  const uint32_t tiles = row_tiles(N);
   p.all_steps = static_cast<uint32_t>((K + kStepK - 1) / kStepK);
   const GemvPlan plan = plan_gemv(tiles, p.all_steps, static_cast<uint32_t>(M), static_cast<uint32_t>(mats),
                                   static_cast<uint32_t>(sms));
@@ -754,6 +757,22 @@ nvfp4_status gemv_impl(const char* fn, const void* x, int64_t M, int64_t K, int6
 using namespace nvfp4;
 
 extern "C" {
+
+int nvfp4_testing_gemv_plan(int64_t M, int64_t N, int64_t K, int weights, int sms, int plan[5]) {
+  if (M < 1 || M > kMaxTokens || N < 1 || N > (1ll << 30) || K < 64 || K % 64 != 0 || K > (1ll << 24) || weights < 1 ||
+      weights > 2 || sms < 1)
+    return 0;
+  const uint32_t steps = static_cast<uint32_t>((K + kStepK - 1) / kStepK);
+  const GemvPlan g = plan_gemv(row_tiles(N), steps, static_cast<uint32_t>(M), static_cast<uint32_t>(weights),
+                               static_cast<uint32_t>(sms));
+  const uint32_t part = (steps + g.ranks - 1) / g.ranks;
+  plan[0] = static_cast<int>(g.grid);
+  plan[1] = static_cast<int>(g.ranks);
+  plan[2] = static_cast<int>(g.piece_steps);
+  plan[3] = static_cast<int>((part + g.piece_steps - 1) / g.piece_steps);
+  plan[4] = static_cast<int>(g.depth);
+  return g.grid > 0;
+}
 
 nvfp4_status nvfp4_gemv(const void* x, int64_t M, int64_t K, int64_t ldx, const void* w_codes, const void* w_scales,
                         const float* w_global, int64_t N, void* y, int64_t ldy, int out_dtype, void* stream) {
