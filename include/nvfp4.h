@@ -371,7 +371,10 @@ NVFP4_API nvfp4_status nvfp4_quantize_arc_rmsnorm_gemm(const void* x, int64_t M,
  * NVFP4 weight: the activations are not quantized.
  *   y[m, n] = alpha_W * sum_k x[m, k] * s[n, k/16] * q[n, k]
  * with exact products, a binary32 sum in a fixed order and one rounding to
- * the output type.  Inf and NaN in x act as in that sum.
+ * the output type.  x is held exactly where |x| is at least 2^-31 of the largest
+ * finite one among the same 256 columns (0..255, 256..511, ...) of its row, and
+ * within 2^-39 of that largest one where it is smaller, whatever the weights are.
+ * Inf and NaN in x act as in that sum.
  *   x        bf16 [M, K], 1 <= M <= 16, row stride ldx >= K elements (a base
  *            and row pitch of 16 bytes load fastest; none is needed)
  *   w_*      the weight [N, K] as nvfp4_quantize writes it

@@ -899,7 +899,8 @@ def _output(out, out_dtype, M: int, N: int, like):
 def gemv(x, w: NVFP4Tensor, out_dtype=None, out=None, stream=None):
     """y [M, N] = x @ W_hat^T for 1 to 16 bf16 CUDA rows x [M, K] against the
     NVFP4 weight ``w`` [N, K]: the decode form of a linear layer, with the
-    activations left in bf16.  More rows: ``quantize_gemm``."""
+    activations left in bf16 (elements below 2^-31 of the largest of their 256
+    columns are held within 2^-39 of it).  More rows: ``quantize_gemm``."""
     if stream is None and (_F or _fast()):
         y = _F.gemv(x, w, out_dtype, out)
         if y is not None:
