@@ -101,7 +101,8 @@ typedef enum { NVFP4_MODE_SIX = 0, NVFP4_MODE_FOUR_OVER_SIX = 1 } nvfp4_mode;
 typedef enum { NVFP4_RULE_MAX = 0, NVFP4_RULE_MAE = 1, NVFP4_RULE_MSE = 2 } nvfp4_rule;
 typedef enum { NVFP4_OUT_BF16 = 0, NVFP4_OUT_FP32 = 1 } nvfp4_out_dtype;
 /* Activation of the gated feed-forward block: act(g) = g * sigma(g) (SiLU) or
- * the tanh form of GELU, g * sigma(2 c (g + 0.044715 g^3)), c = sqrt(2 / pi). */
+ * the tanh form of GELU, g * sigma(2 c (g + 0.044715 g^3)), c = sqrt(2 / pi).  A
+ * sigma below 2^-126 counts as 0. */
 typedef enum { NVFP4_ACT_SILU = 0, NVFP4_ACT_GELU = 1 } nvfp4_act;
 
 /* Bytes of the packed code buffer: rows * K / 2. */

@@ -15,11 +15,12 @@ namespace nvfp4 {
 //         (1 + tanh(a)) / 2 = sigma(2a)
 // and act'(g) = sigma + g sigma (1 - sigma) z'(g).
 //
-// sigma takes the hardware's exponential and reciprocal (1 + exp(-z) is never
-// below 1, so flushing subnormals changes nothing): relative to sigma the
-// exponential is off by 2^-22 and |z| 2^-23, the reciprocal by 2^-23.  Where |z|
-// is large and z negative that is |z| 2^-23 of a vanishing sigma, elsewhere
-// below 2^-20 together.  An exp(-z) past the range gives sigma = 0.
+// sigma takes the hardware's exponential and reciprocal: relative to sigma the
+// exponential is off by 2^-22 and |z| 2^-22 (the roundings of -z log2(e)), the
+// reciprocal by 2^-23.  Where |z| is large and z negative that is |z| 2^-22 of a
+// vanishing sigma, elsewhere below 2^-20 together.  The reciprocal flushes a
+// subnormal result, so sigma below 2^-126 (z below -87.34) counts as 0: act(g) is
+// then 0 and off by less than |g| 2^-126, act'(g) by less than (1 + |g| z') 2^-126.
 constexpr float kGelu2C = 1.5957691216057308f;  // 2c
 constexpr float kGeluCubic = 0.044715f;
 constexpr float kLog2e = 1.4426950408889634f;
