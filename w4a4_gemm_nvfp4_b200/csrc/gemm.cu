@@ -81,8 +81,8 @@ constexpr uint32_t OFF_B = OFF_A + STAGES * A_STAGE;
 constexpr uint32_t OFF_SFA = OFF_B + STAGES * B_STAGE;
 constexpr uint32_t OFF_SFB = OFF_SFA + STAGES * SFA_STAGE;
 constexpr uint32_t OFF_BAR = OFF_SFB + STAGES * SFB_STAGE;
-// full[], empty[], acc_full, acc_free, drain; gated checkpoints: 2 per quad
-constexpr uint32_t NUM_BARS = 2 * STAGES + 3 + 8;
+// full[], empty[], acc_full, acc_free, drain; gated checkpoints: 2 x 2 per quad
+constexpr uint32_t NUM_BARS = 2 * STAGES + 3 + 16;
 constexpr uint32_t OFF_MISC = OFF_BAR + NUM_BARS * 8;
 // epilogue staging for TMA stores: per epilogue warp two 32-row x 128-byte
 // buffers (1024-byte aligned for the 128-byte swizzle)
@@ -542,7 +542,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
   const uint32_t bar_acc_full = bar_empty + 8 * STAGES;
   const uint32_t bar_acc_free = bar_acc_full + 8;
   const uint32_t bar_drain = bar_acc_free + 8;
-  const uint32_t bar_ck = bar_drain + 8;  // [quad][slot]
+  const uint32_t bar_ck = bar_drain + 8;     // [quad][slot]: the slot is written
+  const uint32_t bar_ck_read = bar_ck + 64;  // [quad][slot]: it is read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
 
@@ -559,7 +560,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     mbar_init(bar_acc_free, GATED ? 32 : 8);  // one arrive per epilogue warp of both CTAs
     mbar_init(bar_drain, 1);
     if (EPI == kEpiGatedCkpt && !SMALL)
-      for (int i = 0; i < 8; ++i) mbar_init(bar_ck + 8 * i, 3);
+      for (int i = 0; i < 8; ++i) {
+        mbar_init(bar_ck + 8 * i, 3);
+        mbar_init(bar_ck_read + 8 * i, 1);
+      }
     *abort = 0;
     fence_barrier_init();
   }
@@ -839,9 +843,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         // three of them hand theirs to the first, which stores 8 bytes at once
         // (8192 x 17408 x 5120: 2-byte stores cost 35 us, these 11).  The
         // slots alternate with the tiles that reach this point, which are the same
-        // for all four (a tile whose rows lie past M uses none): a warp is here for
-        // the second of them after a tile only when the first warp has arrived for
-        // a later tile, and so has used what it read from the first.
+        // for all four (a tile whose rows lie past M uses none).  Each has a barrier
+        // for either direction: the first warp reads once all three have written, and
+        // they write again once it has read (the accumulator's hand-over does not
+        // order that: its arrive is relaxed).
         if (EPI == kEpiGatedCkpt) {
           const int blk = col0 / kCkptBlock;
           uint16_t* at = p.ck_scales + static_cast<int64_t>(row) * p.ck_blocks + blk;
@@ -849,8 +854,14 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           if (p.ck_blocks % 4 == 0) {
             const uint32_t slot = static_cast<uint32_t>(quad * 2) + (handed & 1u), hand_phase = (handed >> 1) & 1u;
             ++handed;
+            const bool again = handed > 2;  // the slot has been used before
             uint32_t* hand = reinterpret_cast<uint32_t*>(smem + OFF_CKS + slot * CKS_SLOT) + lane;
             if (sub > 0) {
+              ok = !again || mbar_wait_bounded(bar_ck_read + 8 * slot, hand_phase ^ 1u, abort, p.timeout_ns);
+              if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0 && !*abort) record_timeout(p, abort, 6);
+                break;
+              }
               hand[(sub - 1) * 32] = own;
               __syncwarp();
               if (lane == 0) mbar_arrive(bar_ck + 8 * slot);
@@ -861,6 +872,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
                 break;
               }
               const uint32_t s1 = hand[0], s2 = hand[32], s3 = hand[64];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_ck_read + 8 * slot);
               if (row < p.M) {
                 *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(own, s1, 0x5410), __byte_perm(s2, s3, 0x5410));
                 *reinterpret_cast<uint2*>(at + up) =
