@@ -39,7 +39,7 @@ struct BackwardParams {
   uint16_t* h;             // or null
   int64_t ldh;
   int64_t rows;
-  int cols, blocks, act;
+  int cols, blocks;
   uint32_t chunks;         // groups of columns in a row, one per thread (or warp)
   uint32_t step_chunks;    // the grid's stride in (rows, chunks)
   int64_t step_rows;
@@ -55,19 +55,40 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // an exact zero, and that times an infinite z' would be NaN instead of 0.
 constexpr float kSquareCap = 1.0e18f;
 
-struct Gate {
-  float act, grad;
-};
-// act(g) and act'(g)
-__device__ __forceinline__ Gate gate_of(float g, int act) {
-  const float s = gate_sigma(g, act);
-  const float a = g * s;
-  const float dz = act == NVFP4_ACT_SILU ? 1.0f : kGelu2C * fmaf(3.0f * kGeluCubic, fminf(g * g, kSquareCap), 1.0f);
-  return {a, fmaf(a * (1.0f - s), dz, s)};
-}
-
 __device__ __forceinline__ float code_value(uint32_t word, int i) {
   return static_cast<float>(static_cast<int8_t>(word >> (8 * i)));
+}
+
+// dg, du and h of a pair of columns, in packed binary32: every kernel's, so that they
+// agree bit for bit.  The activation is a constant (a branch on it for each pair:
+// 8192 x 14333 220 us against 199, with GELU and h 267 against 256).
+template <int ACT>
+__device__ __forceinline__ void gate2(const f2& d, const f2& g, const f2& u, f2& vg, f2& vu, f2& vh) {
+  const f2 one = make_f2(1.0f, 1.0f);
+  const auto sigma = [&](const f2& t) {  // t = -z log2(e)
+    const f2 e = add2(make_f2(ex2_approx(t.a()), ex2_approx(t.b())), one);
+    return make_f2(rcp_approx(e.a()), rcp_approx(e.b()));
+  };
+  const auto less = [&](const f2& s) { return fma2(s, make_f2(-1.0f, -1.0f), one); };  // 1 - sigma
+  // act' = sigma + g sigma (1 - sigma) z', the last product and the sum in one rounding,
+  // said so: left to the compiler it was one in one kernel and two in another
+  f2 s, a, slope;
+  if constexpr (ACT == NVFP4_ACT_SILU) {
+    s = sigma(mul2(g, make_f2(-kLog2e, -kLog2e)));
+    a = mul2(g, s);
+    slope = fma2(a, less(s), s);
+  } else {
+    f2 gg = mul2(g, g);
+    gg = make_f2(fminf(gg.a(), kSquareCap), fminf(gg.b(), kSquareCap));
+    s = sigma(mul2(g, fma2(gg, make_f2(kGeluT3, kGeluT3), make_f2(kGeluT1, kGeluT1))));
+    a = mul2(g, s);
+    slope = fma2(mul2(a, less(s)),
+                 fma2(gg, make_f2(3.0f * kGelu2C * kGeluCubic, 3.0f * kGelu2C * kGeluCubic), make_f2(kGelu2C, kGelu2C)), s);
+  }
+  // u act'(g) first: dh u alone may leave the range that the gradient is in
+  vg = mul2(d, mul2(u, slope));
+  vu = mul2(d, a);
+  vh = mul2(a, u);
 }
 
 // Eight columns: dh as four words, the codes and scales of g and u.
@@ -79,8 +100,9 @@ struct Eight {
 
 // dg, du and h of eight columns in packed binary32, rounded to bf16: four words
 // each.
-__device__ __forceinline__ void gate8(const Eight& c, int act, uint32_t* dg, uint32_t* du, uint32_t* h) {
-  const f2 gs = make_f2(c.gs, c.gs), us = make_f2(c.us, c.us), one = make_f2(1.0f, 1.0f);
+template <int ACT>
+__device__ __forceinline__ void gate8(const Eight& c, uint32_t* dg, uint32_t* du, uint32_t* h) {
+  const f2 gs = make_f2(c.gs, c.gs), us = make_f2(c.us, c.us);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t gw = i < 2 ? c.gq.x : c.gq.y, uw = i < 2 ? c.uq.x : c.uq.y;
@@ -88,22 +110,8 @@ __device__ __forceinline__ void gate8(const Eight& c, int act, uint32_t* dg, uin
     const f2 d = make_f2(__uint_as_float(c.dh[i] << 16), __uint_as_float(c.dh[i] & 0xFFFF0000u));
     const f2 g = mul2(gs, make_f2(code_value(gw, b), code_value(gw, b + 1)));
     const f2 u = mul2(us, make_f2(code_value(uw, b), code_value(uw, b + 1)));
-    f2 t, dz, gg;
-    if (act == NVFP4_ACT_SILU) {
-      t = mul2(g, make_f2(-kLog2e, -kLog2e));
-    } else {
-      gg = mul2(g, g);
-      gg = make_f2(fminf(gg.a(), kSquareCap), fminf(gg.b(), kSquareCap));
-      t = mul2(g, fma2(gg, make_f2(kGeluT3, kGeluT3), make_f2(kGeluT1, kGeluT1)));
-      dz = fma2(gg, make_f2(3.0f * kGelu2C * kGeluCubic, 3.0f * kGelu2C * kGeluCubic), make_f2(kGelu2C, kGelu2C));
-    }
-    const f2 e = add2(make_f2(ex2_approx(t.a()), ex2_approx(t.b())), one);
-    const f2 s = make_f2(rcp_approx(e.a()), rcp_approx(e.b()));
-    const f2 a = mul2(g, s);
-    f2 as = mul2(a, fma2(s, make_f2(-1.0f, -1.0f), one));  // g sigma (1 - sigma)
-    if (act != NVFP4_ACT_SILU) as = mul2(as, dz);
-    // u act'(g) first: dh u alone may leave the range that the gradient is in
-    const f2 vg = mul2(d, mul2(u, add2(as, s))), vu = mul2(d, a), vh = mul2(a, u);
+    f2 vg, vu, vh;
+    gate2<ACT>(d, g, u, vg, vu, vh);
     dg[i] = pack2(vg.a(), vg.b());
     du[i] = pack2(vu.a(), vu.b());
     h[i] = pack2(vh.a(), vh.b());
@@ -112,6 +120,7 @@ __device__ __forceinline__ void gate8(const Eight& c, int act, uint32_t* dg, uin
 
 // Every row of dh, dgu and h starts on 16 bytes and 8 divides the columns: 8
 // columns per thread, two such chunks in flight.
+template <int ACT>
 __global__ void __launch_bounds__(kThreads) gated_backward_kernel(const BackwardParams p) {
   pdl_launch_dependents();
   pdl_wait();  // the launch overlaps the previous kernel's tail
@@ -136,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) gated_backward_kernel(const Backward
   };
   auto finish = [&](const Eight& c, int64_t r, uint32_t ch) {
     uint32_t dg[4], du[4], h[4];
-    gate8(c, p.act, dg, du, h);
+    gate8<ACT>(c, dg, du, h);
     uint16_t* g = p.dgu + r * p.ldg + ch * 8;
     *reinterpret_cast<uint4*>(g) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
     *reinterpret_cast<uint4*>(g + p.cols) = make_uint4(du[0], du[1], du[2], du[3]);
@@ -159,6 +168,7 @@ __global__ void __launch_bounds__(kThreads) gated_backward_kernel(const Backward
 }
 
 // One column per thread: narrow matrices at any alignment.
+template <int ACT>
 __global__ void __launch_bounds__(kThreads) gated_backward_narrow_kernel(const BackwardParams p) {
   pdl_launch_dependents();
   pdl_wait();  // the launch overlaps the previous kernel's tail
@@ -168,14 +178,15 @@ __global__ void __launch_bounds__(kThreads) gated_backward_narrow_kernel(const B
   uint32_t col = static_cast<uint32_t>(first - row * p.chunks);
   while (row < p.rows) {
     const int64_t ur = p.rows + row;
-    const float d = bf16_to_f32(p.dh[row * p.ldd + col]);
-    const float g = bf16_to_f32(p.scales[row * p.blocks + col / kCkptBlock]) * p.codes[row * pitch + col];
-    const float u = bf16_to_f32(p.scales[ur * p.blocks + col / kCkptBlock]) * p.codes[ur * pitch + col];
-    const Gate t = gate_of(g, p.act);
+    const f2 gs = make_f2(bf16_to_f32(p.scales[row * p.blocks + col / kCkptBlock]), 0.0f);
+    const f2 us = make_f2(bf16_to_f32(p.scales[ur * p.blocks + col / kCkptBlock]), 0.0f);
+    f2 vg, vu, vh;
+    gate2<ACT>(make_f2(bf16_to_f32(p.dh[row * p.ldd + col]), 0.0f), mul2(gs, make_f2(p.codes[row * pitch + col], 0.0f)),
+               mul2(us, make_f2(p.codes[ur * pitch + col], 0.0f)), vg, vu, vh);
     uint16_t* out = p.dgu + row * p.ldg + col;
-    out[0] = static_cast<uint16_t>(pack2(d * (u * t.grad), 0.0f));
-    out[p.cols] = static_cast<uint16_t>(pack2(d * t.act, 0.0f));
-    if (p.h) p.h[row * p.ldh + col] = static_cast<uint16_t>(pack2(t.act * u, 0.0f));
+    out[0] = static_cast<uint16_t>(pack2(vg.a(), 0.0f));
+    out[p.cols] = static_cast<uint16_t>(pack2(vu.a(), 0.0f));
+    if (p.h) p.h[row * p.ldh + col] = static_cast<uint16_t>(pack2(vh.a(), 0.0f));
     row += p.step_rows;
     col += p.step_chunks;
     if (col >= p.chunks) col -= p.chunks, ++row;
@@ -278,6 +289,7 @@ __device__ __forceinline__ void store_row8(uint16_t* row, int col, int cols, uin
   }
 }
 
+template <int ACT>
 __global__ void __launch_bounds__(kThreads) gated_backward_rows_kernel(const BackwardParams p) {
   pdl_launch_dependents();
   pdl_wait();  // the launch overlaps the previous kernel's tail
@@ -300,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) gated_backward_rows_kernel(const Bac
     }
     load_row8(p.dh + row * p.ldd, col, p.cols, lane, inside, c.dh);
     uint32_t dg[4], du[4], h[4];
-    gate8(c, p.act, dg, du, h);
+    gate8<ACT>(c, dg, du, h);
     uint16_t* out = p.dgu + row * p.ldg;
     store_row8(out, col, p.cols, lane, inside, dg);
     store_row8(out + p.cols, col, p.cols, lane, inside, du);
@@ -328,18 +340,19 @@ unsigned spread(BackwardParams& p, int sms, int64_t cols, int width, int per_cta
 // N: columns; wide: every row on 16 bytes and 8 divides N.  256 columns are a
 // warp's segment in the rows kernel; below that most of its lanes would idle
 // (8192 x 130: 14.4 us against 12.3, 8192 x 999: 33 against 49).
+template <int ACT>
 cudaError_t launch_backward(BackwardParams& p, bool wide, int sms, cudaStream_t s) {
   if (wide) {
     const unsigned grid = spread(p, sms, p.cols, 8, kThreads);
-    return launch_kernel(gated_backward_kernel, dim3(grid), dim3(kThreads), 0, s, true, p);
+    return launch_kernel(gated_backward_kernel<ACT>, dim3(grid), dim3(kThreads), 0, s, true, p);
   }
   if (p.cols >= 256) {
     // (a row's last vector may start up to 7 columns early)
     const unsigned grid = spread(p, sms, static_cast<int64_t>(p.cols) + 7, kSegStep, kThreads / 32);
-    return launch_kernel(gated_backward_rows_kernel, dim3(grid), dim3(kThreads), 0, s, true, p);
+    return launch_kernel(gated_backward_rows_kernel<ACT>, dim3(grid), dim3(kThreads), 0, s, true, p);
   }
   const unsigned grid = spread(p, sms, p.cols, 1, kThreads);
-  return launch_kernel(gated_backward_narrow_kernel, dim3(grid), dim3(kThreads), 0, s, true, p);
+  return launch_kernel(gated_backward_narrow_kernel<ACT>, dim3(grid), dim3(kThreads), 0, s, true, p);
 }
 
 }  // namespace
@@ -389,11 +402,11 @@ nvfp4_status nvfp4_gated_backward(const void* dh, int64_t ldd, const void* ckpt_
   p.rows = M;
   p.cols = static_cast<int>(N);
   p.blocks = static_cast<int>((N + kCkptBlock - 1) / kCkptBlock);
-  p.act = act;
   const bool wide = N % 8 == 0 && aligned16(dh) && aligned16(dgu) && ldd % 8 == 0 && ldg % 8 == 0 &&
                     (!h || (aligned16(h) && ldh % 8 == 0));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_backward(p, wide, sms, s);
+  const cudaError_t e = act == NVFP4_ACT_SILU ? launch_backward<NVFP4_ACT_SILU>(p, wide, sms, s)
+                                              : launch_backward<NVFP4_ACT_GELU>(p, wide, sms, s);
   if (e != cudaSuccess) return cuda_status(e, "gated_backward_kernel launch");
   return NVFP4_OK;
 }
