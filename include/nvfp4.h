@@ -415,7 +415,7 @@ NVFP4_API nvfp4_status nvfp4_gemv_gated(const void* x, int64_t M, int64_t K, int
  *                 with B = ceil(N / 32) (nvfp4_checkpoint_codes_bytes,
  *                 nvfp4_checkpoint_scales_bytes), gate first.  Block b of a row
  *                 holds columns 32 b .. 32 b + 31 (zeros past N) as
- *                 q = rint(v * fl(1 / s)), to even, with
+ *                 q = rint(v * fl(1 / s)), the product exact, to even, with
  *                 s = the least bf16 >= max(fl(max|v| / 127), 2^-100), so that
  *                 a value reads back as s * q within s / 2; a block that holds
  *                 Inf or NaN gets s = NaN and reads back as NaN.

@@ -47,3 +47,23 @@ def test_many_calls_back_to_back():
     kept = [nv.gemm_gated(a, wg, wu, checkpoint=True)[1] for _ in range(30)]
     torch.cuda.synchronize()
     assert all(torch.equal(k.scales, ref.scales) and torch.equal(k.codes, ref.codes) for k in kept)
+
+
+@pytest.mark.parametrize("shape", [(1300, 9600, 256), (1300, 9632, 64), (300, 2304, 256), (2048, 14336, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_codes_and_scales_are_those_of_the_products(shape):
+    """From the products as nvfp4_gemm writes them, bit for bit and in every kernel
+    (small and wide tiles, outputs on and off 16 bytes): the scale rounded up, the code
+    one rounding of the exact v * fl(1 / s)."""
+    M, N, K = shape
+    a, wg, wu = operand(M, K, 1), operand(N, K, 2), operand(N, K, 3)
+    for pitch in (N, N + 1):
+        _, ck = nv.gemm_gated(a, wg, wu, checkpoint=True,
+                              out=torch.zeros(M, pitch, dtype=torch.bfloat16, device="cuda")[:, :N])
+        for i, w in enumerate((wg, wu)):
+            v = nv.gemm(a, w, out_dtype=torch.float32).view(M, N // 32, 32)
+            t = (v.abs().amax(-1) / 127.0).clamp(min=2.0 ** -100)
+            s = ((t.view(torch.int32) + 0xFFFF) & -0x10000).view(torch.float32)
+            q = torch.round(v.double() * (1.0 / s).double()[..., None])
+            assert torch.equal(ck.scales[i].float(), s)
+            assert torch.equal(ck.codes[i][:, :N], q.view(M, N).to(torch.int8))

@@ -60,7 +60,8 @@ __device__ __forceinline__ float ckpt_scale(float amax) {
 }
 
 // Adding 1.5 * 2^23 to a number below 2^22 rounds it to the nearest whole one,
-// ties to even, and leaves that in the low byte.
+// ties to even, and leaves that in the low byte; in an FMA the number is an exact
+// product.
 constexpr float kCkptRound = 12582912.0f;
 
 }  // namespace nvfp4

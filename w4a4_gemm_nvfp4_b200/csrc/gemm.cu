@@ -347,8 +347,9 @@ __device__ __forceinline__ f2 act_mul2(f2 g, f2 u, int act) {
   return mul2(mul2(g, make_f2(rcp_approx(d.a()), rcp_approx(d.b()))), u);
 }
 
-// One block of a row as 8-bit codes q = rint(v * (1 / s)), four to a word, into
-// shared memory at `lo` and `hi` (16 bytes each); its scale s, as bf16 bits.
+// One block of a row as 8-bit codes q = rint(v * fl(1 / s)), the exact product in
+// one rounding, four to a word, into shared memory at `lo` and `hi` (16 bytes each);
+// its scale s, as bf16 bits.
 __device__ __forceinline__ uint16_t checkpoint_block(const f2* x, uint32_t lo_at, uint32_t hi_at) {
   float m = 0.0f;
 #pragma unroll
@@ -357,8 +358,8 @@ __device__ __forceinline__ uint16_t checkpoint_block(const f2* x, uint32_t lo_at
   uint32_t q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const f2 lo = add2(mul2(x[2 * i], make_f2(inv, inv)), make_f2(kCkptRound, kCkptRound));
-    const f2 hi = add2(mul2(x[2 * i + 1], make_f2(inv, inv)), make_f2(kCkptRound, kCkptRound));
+    const f2 lo = fma2(x[2 * i], make_f2(inv, inv), make_f2(kCkptRound, kCkptRound));
+    const f2 hi = fma2(x[2 * i + 1], make_f2(inv, inv), make_f2(kCkptRound, kCkptRound));
     q[i] = __byte_perm(__byte_perm(__float_as_uint(lo.a()), __float_as_uint(lo.b()), 0x0040),
                        __byte_perm(__float_as_uint(hi.a()), __float_as_uint(hi.b()), 0x0040), 0x5410);
   }
