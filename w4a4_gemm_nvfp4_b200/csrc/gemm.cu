@@ -222,7 +222,6 @@ struct GemmParams {
   uint32_t m_tiles;       // ceil(M / 256)
   uint32_t num_tiles;     // ceil(M / 256) * n_tiles
   int out_fp32;
-  int vec_store;          // rows of Y start 16-byte aligned: vector stores
   int tma_store;          // Y base and row pitch 16-byte aligned: TMA stores through shared memory
   // NVFP4 output (epilogue kinds 1..4): Y quantized with a caller-supplied alpha
   const float* q_alpha;
@@ -311,30 +310,16 @@ __device__ __forceinline__ void store_tile_row(const CUtensorMap& tmY, const Gem
   }
   // direct stores (Y not 16-byte aligned or pitched): one row per lane
   if (row >= p.M) return;
-  const bool full = p.vec_store && col0 + static_cast<int>(EPI_N) <= p.N;
   if (p.out_fp32) {
     float* dst = static_cast<float*>(p.y) + static_cast<int64_t>(row) * p.ldy + col0;
-    if (full) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 4)
-        *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (col0 + i < p.N) dst[i] = v[i];
-    }
+    for (int i = 0; i < 64; ++i)
+      if (col0 + i < p.N) dst[i] = v[i];
   } else {
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.y) + static_cast<int64_t>(row) * p.ldy + col0;
-    if (full) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 8)
-        *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
-                                                        pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (col0 + i < p.N) dst[i] = __float2bfloat16_rn(v[i]);
-    }
+    for (int i = 0; i < 64; ++i)
+      if (col0 + i < p.N) dst[i] = __float2bfloat16_rn(v[i]);
   }
 }
 
@@ -1208,8 +1193,7 @@ nvfp4_status gemm_prepare(GemmLaunch* L, const char* fn, const void* a_codes, co
   if (num_tiles > 0x7FFFFFFFll) return set_error(NVFP4_ERR_INVALID_ARG, "%s: too many tiles", fn);
   p.num_tiles = static_cast<uint32_t>(num_tiles);
   p.out_fp32 = out_dtype == NVFP4_OUT_FP32;
-  p.vec_store = aligned16(y) && ((ldy * (p.out_fp32 ? 4 : 2)) % 16 == 0);
-  p.tma_store = p.vec_store && epi == 0;
+  p.tma_store = epi == 0 && aligned16(y) && ((ldy * (p.out_fp32 ? 4 : 2)) % 16 == 0);
   p.u_global = nullptr;
   p.act = 0;
   p.ck_codes = nullptr;
