@@ -168,6 +168,21 @@ def test_a_stream_of_another_device_is_refused(name, monkeypatch):
     assert not m.calls
 
 
+@pytest.mark.parametrize("name", [n for n in CALLS if n.startswith(("quantize", "gemm")) and "gated" not in n])
+def test_a_stream_may_be_any_object_with_a_handle(name, monkeypatch):
+    """(The decode and gated calls ask for the stream's device.)"""
+    class Handle:
+        cuda_stream = 11
+
+    fn, args, kw = CALLS[name]()
+    m = Machine(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda handle: m.side if handle == m.side.cuda_stream else m.main)
+    assert m.side.cuda_stream == Handle.cuda_stream
+    fn(*args, **kw, stream=Handle())
+    assert m.calls == [m.side.cuda_stream] and set(m.pool.values()) <= {m.side}
+
+
 # ------------------------------------------------------------- on the GPU --
 
 def weight(rows, k):

@@ -336,6 +336,8 @@ def _on_stream(fn):
             return fn(*args, **kwargs)
         import torch
 
+        if not hasattr(stream, "device"):  # any object with a cuda_stream handle
+            stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
         current = torch.cuda.current_stream(stream.device)
         if stream == current:
             return fn(*args, **kwargs)
