@@ -229,3 +229,37 @@ def test_an_input_dropped_after_the_call_is_kept_for_its_stream():
             torch.ones(shape, dtype=dtype, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(got, ref)
+
+
+@pytest.mark.gpu
+def test_captured_on_a_forked_stream():
+    """A capture that forks to another stream and joins it again, results and
+    temporaries dropped inside it."""
+    a, wg, wu = weight(64, 512), weight(320, 512), weight(320, 512)
+    x, dh = (torch.randn(64, n, device="cuda").to(torch.bfloat16) for n in (512, 320))
+    side = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        h, ck = nv.gemm_gated(a, wg, wu, checkpoint=True, stream=side)
+        dgu = nv.gated_backward(dh, ck, stream=side)
+        del ck
+        q = nv.quantize(x, stream=side)
+        y = nv.gemm(q, wg, stream=side)
+        del q
+        z = nv.gemv(x[:5], wu, stream=side)
+        main.wait_stream(side)
+        return h, dgu, y, z
+
+    ref = [t.clone() for t in work()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, ref))
