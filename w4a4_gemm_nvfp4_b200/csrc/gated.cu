@@ -11,11 +11,11 @@
 // needs, can be written again in the same pass instead of being kept.
 //
 // Nothing is used twice, so the kernel is bound by HBM: 2 + 2 (1 + 1/16) bytes
-// in and 4 (6 with h) out per element (8192 x 14336: 162 us, 90 % of a copy's
-// rate, 193 us and 94 % with h).  About 20 operations an element in packed
+// in and 4 (6 with h) out per element (8192 x 14336: 159 us, 91 % of a copy's
+// rate, 190 us and 95 % with h).  About 20 operations an element in packed
 // binary32 hide behind that; results are rounded once, to bf16.  Rows off 16-byte
 // alignment are put together in registers and bound by issue: 8192 x 14333 takes
-// 223 us, 256 with h.
+// 199 us, 232 with h.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(kThreads) gated_backward_rows_kernel(const Bac
 
 // Chunks of `width` columns, `per_cta` of them for a CTA at a time.  Up to 32 CTAs
 // per SM: a few waves even out what each of them meets in HBM (8192 x 14336 with
-// h: 221 us with 8, 205 with 16, 193 with 32, 225 with one chunk or two per
-// thread).
+// h, when they were compared: 221 us with 8, 205 with 16, 193 with 32, 225 with one
+// chunk or two per thread).
 unsigned spread(BackwardParams& p, int sms, int64_t cols, int width, int per_cta) {
   p.chunks = static_cast<uint32_t>((cols + width - 1) / width);
   const int64_t total = p.rows * p.chunks;
@@ -339,7 +339,7 @@ unsigned spread(BackwardParams& p, int sms, int64_t cols, int width, int per_cta
 
 // N: columns; wide: every row on 16 bytes and 8 divides N.  256 columns are a
 // warp's segment in the rows kernel; below that most of its lanes would idle
-// (8192 x 130: 14.4 us against 12.3, 8192 x 999: 33 against 49).
+// (8192 x 130: 9.4 us against 6.9, 8192 x 999: 26.9 against 31.6).
 template <int ACT>
 cudaError_t launch_backward(BackwardParams& p, bool wide, int sms, cudaStream_t s) {
   if (wide) {

@@ -44,10 +44,11 @@
 // CTA with a part of K, and their sums are added in the order of the CTAs.
 //
 // Measured (device time, weights from HBM): 1 x 14336 x 4096 9.4 us (3.5 TB/s;
-// about 4 us of it launch, x and the last sum), the gated form 15.7 us (4.2
-// TB/s), 5 x 12283 x 5120 13 us, gated 16 x 17408 x 5120 28.7 us (3.5 TB/s; there
-// issue bounds it: a unit of 16 x 256 weights takes 286 warp instructions with
-// one column tile of tokens and 380 with two).
+// about 3 us of it launch, x and the last sum), the gated form 15.7 us (4.2
+// TB/s), 5 x 12283 x 5120 13 us (3 us of it x), gated 16 x 17408 x 5120 28.7 us
+// (3.5 TB/s; there the stream takes 22 us, 15 with its loads alone and 18 with its
+// arithmetic alone, 380 warp instructions for a unit of 16 x 256 weights, 286 with one
+// column tile of tokens), 16 x 5120 x 17408 32 us (half of it x, in four pieces).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
